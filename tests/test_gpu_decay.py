@@ -30,7 +30,7 @@ CASES = [  # dtype, d, B, T, H, state, lengths
     ("bf16", 128, 2, 300, 3, False, None),
     ("bf16", 128, 5, 200, 2, True, [200, 0, 1, 128, 137]),
     ("bf16", 128, 3, 90, 2, False, [-7, 1000, 33]),          # clamped to [0, T]
-    ("bf16", 128, 1, 1030, 6, True, None),                    # two segments
+    ("bf16", 128, 1, 1030, 6, True, None),                    # five segments
     ("bf16", 128, 3, 1601, 2, True, [1601, 700, 0]),          # segments that a sequence does not reach
     ("bf16", 128, 1, 2048, 1, False, [1025]),
     ("f32", 128, 1, 1, 3, True, None),
