@@ -422,8 +422,10 @@ vdn_status vdn_frames_finish(const vdn_shape* shape, int F_total, int world, int
  * branch's features call vdn_feature_prep first).
  *
  *   q, k, v, out  [B, F*S, H, d] dtype  bf16 with d = 128, fp32 with d = 16 or 128
- *   decay      [H]          fp32   lambda in [0, 1] (not checked; a constant of the layer: it gets no
- *                                  gradient); lambda = 0 keeps the current token alone
+ *   decay      [H]          fp32   lambda in [0, 1] (a constant of the layer: it gets no gradient);
+ *                                  lambda = 0 keeps the current token alone.  Not checked: a negative or
+ *                                  NaN decay makes every result of its head NaN (an empty sequence's
+ *                                  state passes through), here, in the gradients and in vdn_decay_step
  *   state_in   [B, H, d, d] fp32   state before the first token, or NULL (zero)
  *   state_out  [B, H, d, d] fp32   receives the state after the last token, or NULL; may be
  *                                  state_in itself (the state is then carried in place)

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(ScanShape<D>::kUnits * (D / ScanShape<D>::R) *
       n_max = max(n_max, min(decay_tokens(lengths, (int)(other % BH / H), T), ot0 + seg_len) - ot0);
     }
   }
-  const float lambda = decay[h];
+  const float lambda = decay_factor(decay[h]);
   const int part = ut % kParts, row0 = ut / kParts * R;   // rows row0 .. row0 + R - 1, float4 columns kParts i + part
 
   float2 s[R][CC / 2];
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(ScanShape<D>::kUnits * (D / ScanShape<D>::R) *
     const long long step = (kRev ? -1 : 1) * (long long)H * D;
     float* o = kOut ? out + (((long long)b * T + token(tl * kTok)) * H + h) * D + row0 + part : nullptr;
     // reverse: the state enters the first token undecayed
-    float first = kRev && tl == 0 ? 1.f : lambda;
+    float first = kRev && tl == 0 && !isnan(lambda) ? 1.f : lambda;
     int k = 0;
     for (; k + Sh::kUnroll <= kn; k += Sh::kUnroll, first = lambda)
       scan_tokens<D, kOut, Sh::kUnroll>(s, tile[buf][u], k, first, lambda, add, row0, part, o + k * step, step, out_scale);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kStepThreads)
     again = __syncthreads_or(late);
   }
   if (!live) return;
-  const float lambda = decay[h];
+  const float lambda = decay_factor(decay[h]);
   for (int row = b;;) {
     const long long at = ((long long)row * H + h) * D;
     float kv[4], qv[4];

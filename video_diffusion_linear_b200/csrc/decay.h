@@ -59,8 +59,12 @@ cudaError_t launch_decay_step(const vdn_shape& sh, const void* q, const void* k,
                               cudaStream_t stream);
 
 // decay as a power of two: lambda^n = 2^(n l2).  lambda = 0 has l2 = -1e30, so that lambda^0 = 1 and
-// lambda^n = 0 need no branch.
-__device__ __forceinline__ float decay_log2(float lambda) { return fmaxf(log2f(lambda), -1e30f); }
+// lambda^n = 0 need no branch.  A NaN or negative decay is NaN here and in decay_factor, so that every form of
+// the operator shows it in all results of its head (fmaxf alone would take it for zero).
+__device__ __forceinline__ float decay_log2(float lambda) {
+  return lambda >= 0.f ? fmaxf(log2f(lambda), -1e30f) : __int_as_float(0x7fffffff);
+}
+__device__ __forceinline__ float decay_factor(float lambda) { return lambda >= 0.f ? lambda : __int_as_float(0x7fffffff); }
 
 // tokens of sequence b: lengths[b] clamped to [0, T]
 __device__ __forceinline__ int decay_tokens(const int* lengths, int b, int T) {
