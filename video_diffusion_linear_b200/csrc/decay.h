@@ -59,10 +59,12 @@ cudaError_t launch_decay_step(const vdn_shape& sh, const void* q, const void* k,
                               cudaStream_t stream);
 
 // decay as a power of two: lambda^n = 2^(n l2).  lambda = 0 has l2 = -1e30, so that lambda^0 = 1 and
-// lambda^n = 0 need no branch.  A NaN or negative decay is NaN here and in decay_factor, so that every form of
-// the operator shows it in all results of its head (fmaxf alone would take it for zero).
+// lambda^n = 0 need no branch.  A NaN or negative decay is NaN here (the maximum that keeps a NaN; fmaxf drops it)
+// and in decay_factor, so that every form of the operator shows it in all results of its head.
 __device__ __forceinline__ float decay_log2(float lambda) {
-  return lambda >= 0.f ? fmaxf(log2f(lambda), -1e30f) : __int_as_float(0x7fffffff);
+  float l2;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(l2) : "f"(log2f(lambda)), "f"(-1e30f));
+  return l2;
 }
 __device__ __forceinline__ float decay_factor(float lambda) { return lambda >= 0.f ? lambda : __int_as_float(0x7fffffff); }
 
