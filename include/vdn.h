@@ -443,8 +443,9 @@ vdn_status vdn_frames_finish(const vdn_shape* shape, int F_total, int world, int
  * rounding.  On the tensor-core path (bf16) two operands of the output's products are rounded to bf16
  * once: the weights lambda^{t-s} (q_t . k_s) inside a chunk of 128 tokens, and the state before the
  * chunk.  There an infinity or NaN in v inside a sequence reaches every output of its chunk (the fp32
- * path: from its token on).  Results do not depend on what ran before (no atomics).  Calls that may
- * run at the same time, captured graphs among them, need workspaces of their own.  Errors as
+ * path: from its token on).  Results depend neither on what ran before (no atomics) nor on whether
+ * state_out is taken.  Calls that may run at the same time, captured graphs among them, need workspaces of
+ * their own.  Errors as
  * vdn_branch_forward; vdn_shape's conv_width is not used (1 or 3).  VDN_ERR_UNSUPPORTED: other d and
  * dtype, B*H above 2^24, more than 2^30 tokens.
  */
@@ -458,7 +459,9 @@ vdn_status vdn_decay_forward(const vdn_shape* shape, const void* q, const void* 
  * dstate_out = dL/d state_out (NULL: zero).  Written, not accumulated:
  *   dq, dk, dv   [B, F*S, H, d] dtype (rows behind a sequence as `clear` says)
  *   dstate_in    [B, H, d, d]   fp32, or NULL
- * The forward's states are recomputed from k and v; nothing is saved between the calls.
+ * The forward's states are recomputed from k and v; nothing is saved between the calls.  In a call
+ * with a state_in no result depends on which optional outputs are taken.  bf16 without one: asking for
+ * dstate_in keeps the state's gradient more exactly, which can change the last bits of dk and dv.
  * workspace: vdn_decay_backward_workspace_size() bytes.  No output may overlap another
  * buffer. */
 size_t vdn_decay_backward_workspace_size(const vdn_shape* shape);

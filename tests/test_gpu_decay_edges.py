@@ -1,4 +1,4 @@
-"""Decayed attention at the edges of its arguments, on the GPU: decays outside their range."""
+"""Decayed attention at the edges of its arguments, on the GPU: decays outside their range, optional outputs."""
 import pytest
 import torch
 
@@ -36,3 +36,19 @@ def test_a_decay_that_is_no_decay_shows_in_every_result(dtype, d, T, bad):
         assert torch.equal(a[1], b[1])                   # an empty sequence passes its state through
     for a, b in zip(want["step"], got["step"]):
         assert bool(torch.isnan(b[:, 0]).all()) and torch.equal(a[:, 1], b[:, 1])
+
+
+@pytest.mark.parametrize("dtype,d,T", PATHS)
+def test_optional_outputs_change_no_other(dtype, d, T):
+    x = cuda(inputs(32, dtype, 2, T, 2, d))
+    x["decay"] = torch.tensor([0.999, 0.9], device="cuda")
+    args = (x["q"], x["k"], x["v"], x["decay"], x["state"])
+    a, _ = api.decay_forward(*args)
+    b, none = api.decay_forward(*args, want_state=False)
+    assert none is None and torch.equal(a, b)
+    full = api.decay_backward(*args, dout=x["dout"], dfinal=x["dfinal"])
+    assert full["dstate"] is not None
+    grads = {n: torch.empty_like(x["q"]) for n in ("dq", "dk", "dv")}
+    api.decay_backward(*args, dout=x["dout"], dfinal=x["dfinal"], grads=grads)
+    for n in grads:
+        assert torch.equal(full[n], grads[n]), n

@@ -533,7 +533,7 @@ vdn_status vdn_decay_forward(const vdn_shape* shape, const void* q, const void* 
   s.init = state_in;
   s.out_near = s.out_far = sc;
   s.add = 1.f;
-  s.exact_state = state_out != nullptr;
+  s.exact_state = true;   // taken or not: out does not depend on it
   s.clear = clear && lengths;
   s.out = out; s.final = state_out;
   s.status = reinterpret_cast<uint32_t*>(ws + p.status);
@@ -582,6 +582,10 @@ vdn_status vdn_decay_backward(const vdn_shape* shape, const void* q, const void*
   const bool tc = use_tc(sh, VDN_IMPL_AUTO);
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)sh.d);
   char* ws = static_cast<char*>(workspace);
+  // The state's gradient is kept to fp32 rounding where the call has a state, whether its gradient is taken or not, so
+  // that dv and dk do not depend on that.  A call without a state pays for it only when it asks for the gradient
+  // (48360 tokens x 24 heads: 1080 us, else 1000).
+  const bool exact = state_in != nullptr || dstate_in != nullptr;
   float *fs = nullptr, *rs = nullptr;
   DecayScan s{};
   s.B = sh.B; s.H = sh.H; s.T = sh.F * sh.S; s.d = sh.d;
@@ -600,7 +604,7 @@ vdn_status vdn_decay_backward(const vdn_shape* shape, const void* q, const void*
     s.clear_status = false;
     DecayScan r = s;                      // their gradients from the end: scale sum lambda^.. do q^T
     r.y = q; r.z = dout; r.init = dstate_out; r.add = sc; r.reverse = true;
-    r.exact_state = dstate_in != nullptr;
+    r.exact_state = exact;
     if (e == cudaSuccess) e = run_segments(r, p, tc, rs);
   }
   // dq_i = scale S_i^T do_i: the scan of z = k, y = v, whose state is S^T, read by do
@@ -620,7 +624,7 @@ vdn_status vdn_decay_backward(const vdn_shape* shape, const void* q, const void*
   dks.x = v; dks.y = dout; dks.z = q; dks.transposed = true; dks.out = dk;
   if (e == cudaSuccess) e = run_scan(dks, p, tc);
   c.x = k; c.y = q; c.z = dout; c.out = dv; c.final = dstate_in;
-  c.exact_state = dstate_in != nullptr;
+  c.exact_state = exact;
   if (e == cudaSuccess) e = run_scan(c, p, tc);
   return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }

@@ -37,7 +37,7 @@ struct DecayScan {
   bool transposed;             // init / seg_states / final hold S^T
   float out_near, out_far;     // o = out_near (terms inside the chunk) + out_far (terms of the state)
   float add;                   // factor of z y^T
-  bool exact_state;            // a state leaves the call: keep it to fp32 rounding (tensor-core path)
+  bool exact_state;            // the state can leave the call: keep it to fp32 rounding (tensor-core path)
   bool clear;                  // rows of out behind a sequence: to zero (else left as they were)
   void* out;
   float* final;                // [B, H, d, d] or NULL: state after the order's last token

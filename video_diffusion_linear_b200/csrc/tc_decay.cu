@@ -10,8 +10,8 @@
 //
 // Precision.  The state stays in fp32 (registers) and every sum in fp32 (TMEM).  The decayed keys
 // Yd are products of a bf16 and an fp32 number, and their product runs on bf16 operands: as three bf16
-// terms they are good to 2^-23 and the state is an fp32 quantity, which it is where the call returns
-// a state; where it only feeds bf16 outputs, two terms (2^-15) are as good and a third cheaper.
+// terms they are good to 2^-23 and the state is an fp32 quantity, which it is where the state can leave the call
+// (DecayScan::exact_state); where it only feeds bf16 outputs, two terms (2^-15) are as good and a third cheaper.
 // Two operands are rounded to bf16 once, 2^-8 of their size at most, as the output itself is: P, and
 // the state as it enters X S^T.
 //
