@@ -1,8 +1,10 @@
-"""Decayed attention at the edges of its arguments, on the GPU: decays outside their range, optional outputs."""
+"""Decayed attention at the edges of its arguments, on the GPU: decays outside their range, optional outputs, and
+sequences that end at every place of a chunk."""
 import pytest
 import torch
 
-from causal import cuda, inputs
+from causal import cuda, inputs, live, scan_bound, within
+from oracle import causal_oracle as C
 from video_diffusion_linear_b200 import api
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +54,35 @@ def test_optional_outputs_change_no_other(dtype, d, T):
     api.decay_backward(*args, dout=x["dout"], dfinal=x["dfinal"], grads=grads)
     for n in grads:
         assert torch.equal(full[n], grads[n]), n
+
+
+@pytest.mark.parametrize("first", [0, 128, 896])
+def test_sequences_that_end_at_every_place_of_a_chunk(first):
+    """bf16: a sequence that ends inside a chunk before T leaves by another way than whole chunks."""
+    B, T, H, d = 128, first + 131, 1, 128
+    g = torch.Generator("cuda").manual_seed(first)
+    x = {n: torch.randn(B, T, H, d, generator=g, device="cuda").bfloat16() for n in ("q", "k", "v", "dout")}
+    x["q"], x["k"], x["v"], x["dout"] = (t[:1].expand(B, T, H, d).contiguous() for t in x.values())
+    lam = torch.tensor([0.97], device="cuda")
+    counts = [first + 1 + b for b in range(B)]
+    lens = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    out = torch.full_like(x["q"], -77.0)
+    api.decay_forward(x["q"], x["k"], x["v"], lam, lengths=lens, out=out)
+    grads = {n: torch.full_like(x["q"], -77.0) for n in ("dq", "dk", "dv")}
+    api.decay_backward(x["q"], x["k"], x["v"], lam, dout=x["dout"], lengths=lens, grads=grads)
+    m = live(counts, T)
+    ref, _ = C.decay_forward(x["q"][:1], x["k"][:1], x["v"][:1], lam)
+    bound = scan_bound("bf16", ref, x["q"][:1], x["k"][:1], x["v"][:1], lam, None, [T], d ** -0.5)
+    got = out.double().cpu().numpy()
+    assert bool((got[~m] == -77.0).all())
+    for b, n in enumerate(counts):
+        within(got[b, :n], ref[0, :n], bound[0, :n], ("out", b))
+    for b in (0, 1, 14, 15, 16, 62, 63, 64, 100, 126, 127):
+        n = counts[b]
+        one = [x[a][:1, :n] for a in ("q", "k", "v", "dout")]
+        rg = C.decay_backward(one[0], one[1], one[2], lam, one[3])
+        for what, (u, y, z), rev in (("dq", (3, 2, 1), False), ("dk", (2, 3, 0), True), ("dv", (1, 0, 3), True)):
+            bd = scan_bound("bf16", rg[what], one[u], one[y], one[z], lam, None, [n], d ** -0.5, rev)
+            have = grads[what].double().cpu().numpy()[b]
+            assert bool((have[n:] == -77.0).all())
+            within(have[:n], rg[what][0], bd[0], (what, b))

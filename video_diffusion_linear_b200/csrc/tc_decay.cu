@@ -503,13 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&sm.o_free);
       if (by_tma(n)) {
         tc::fence_proxy_async_smem();
-      } else {                            // 16 lanes per row
-        tc::named_bar(1, 32 * kNearWarps);
-        const int t = chunk_t(n);
+      } else {
+        // this warp's own rows and columns, eight lanes per row: a barrier with the other warps could wait for one that
+        // has left its role after a wait ran out
+        const int t = chunk_t(n), c = 8 * half + (lane & 7);
 #pragma unroll 4
-        for (int row = tid >> 4; row < m; row += 2 * kNearWarps)
-          *reinterpret_cast<uint4*>(out + (((long long)b * T + t + row) * H + h) * 128 + 8 * (lane & 15)) =
-              *reinterpret_cast<const uint4*>(stage + tile_chunk(row, lane & 15));
+        for (int row = 32 * quarter + (lane >> 3); row < min(m, 32 * quarter + 32); row += 4)
+          *reinterpret_cast<uint4*>(out + (((long long)b * T + t + row) * H + h) * 128 + 8 * c) =
+              *reinterpret_cast<const uint4*>(stage + tile_chunk(row, c));
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.staged[i]);
