@@ -40,3 +40,13 @@ def test_every_wait_of_a_role_is_bounded(name):
     for m in re.finditer(r"[^;{}]*\bmbar_wait\([^;{]*", body):
         call = m.group(0)
         assert "abort_flag, status)" in call and re.search(r"if \(|return|ok = |&&", call), call
+
+
+@pytest.mark.parametrize("name", ["k_decay_tc", "k_decay_segments_tc"])
+def test_teardown_after_a_timeout_waits_for_the_products(name):
+    """Any warp can be the one that gives up, also after the issuing warp has left its role with products in flight:
+    their drain stands where all have come together, before the tensor memory is freed."""
+    body = kernel_body(name)
+    together, freed = [m.start() for m in re.finditer(r"__syncthreads", body)][1:]
+    drains = [m.start() for m in re.finditer(r"umma_commit\(&sm\.drain\)", body)]
+    assert len(drains) == 1 and together < drains[0] < freed < body.index("tmem_dealloc")

@@ -386,10 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                            has_state(n) || kk > 0 ? 1u : 0u);
         tc::umma_commit(&sm.o_full[i]);
       }
-      if (!ok) {   // leave no product in flight
-        tc::umma_commit(&sm.drain);
-        drain_wait(&sm.drain, 0);
-      }
     }
   } else if (warp == kStoreWarp) {
     // ------------------------------------------------------------ stores of the staged output
@@ -614,6 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc::tc_fence_before();
   __syncthreads();
+  if (sm.abort && warp == kMmaWarp && lane == 0) {   // no product may run on, whichever warp gave up
+    tc::umma_commit(&sm.drain);
+    drain_wait(&sm.drain, 0);
+  }
   if (sm.abort && tid == 0) {   // no copy may land after the CTA has left
     for (int n = max(0, sm.yz_issued - 2); n < sm.yz_issued; ++n) drain_wait(&sm.yz_full[n & 1], (n >> 1) & 1);
     for (int n = max(0, sm.x_issued - 2); n < sm.x_issued; ++n) drain_wait(&sm.x_full[n & 1], (n >> 1) & 1);
@@ -727,10 +727,6 @@ __global__ void __launch_bounds__(kSegThreads, 1)
         tc::umma_commit(&sm.u_full[ub]);
         tc::umma_commit(&sm.empty[s]);
       }
-      if (!ok) {
-        tc::umma_commit(&sm.drain);
-        drain_wait(&sm.drain, 0);
-      }
     }
   } else {
     // half by half, the keys are made while the product of the half before runs; a warp takes 16 channels, 32 tokens
@@ -792,6 +788,10 @@ __global__ void __launch_bounds__(kSegThreads, 1)
 
   tc::tc_fence_before();
   __syncthreads();
+  if (sm.abort && warp == kSegWarps + 1 && lane == 0) {
+    tc::umma_commit(&sm.drain);
+    drain_wait(&sm.drain, 0);
+  }
   if (sm.abort && tid == 0) {
     const int issued = sm.issued;
     for (int s = 0; s < kSegStages && s < issued; ++s) {
