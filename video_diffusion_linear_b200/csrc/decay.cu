@@ -479,6 +479,12 @@ vdn_status decay_shape(const vdn_shape* sh) {
   return VDN_OK;
 }
 
+// bf16 has no form of the scan without the tensor cores (the fp32 kernels would read its buffers as floats)
+vdn_status scan_shape(const vdn_shape* sh) {
+  const vdn_status s = decay_shape(sh);
+  return s == VDN_OK && sh->dtype == VDN_DTYPE_BF16 && !use_tc(*sh, VDN_IMPL_AUTO) ? VDN_ERR_UNSUPPORTED : s;
+}
+
 cudaError_t run_scan(const DecayScan& s, const DecayPlan& p, bool tc) {
   return tc ? launch_decay_scan_tc(s, p) : launch_decay_scan_simt(s, p);
 }
@@ -493,16 +499,16 @@ cudaError_t run_segments(const DecayScan& s, const DecayPlan& p, bool tc, float*
 extern "C" {
 
 size_t vdn_decay_workspace_size(const vdn_shape* shape) {
-  return decay_shape(shape) == VDN_OK ? plan_decay(*shape, false).total : 0;
+  return scan_shape(shape) == VDN_OK ? plan_decay(*shape, false).total : 0;
 }
 size_t vdn_decay_backward_workspace_size(const vdn_shape* shape) {
-  return decay_shape(shape) == VDN_OK ? plan_decay(*shape, true).total : 0;
+  return scan_shape(shape) == VDN_OK ? plan_decay(*shape, true).total : 0;
 }
 
 vdn_status vdn_decay_forward(const vdn_shape* shape, const void* q, const void* k, const void* v, const float* decay,
                              const float* state_in, const int* lengths, int clear, float scale, void* workspace,
                              size_t workspace_bytes, void* out, float* state_out, void* stream) {
-  vdn_status st = decay_shape(shape);
+  vdn_status st = scan_shape(shape);
   if (st != VDN_OK) return st;
   if (!q || !k || !v || !decay || !workspace || !out || !std::isfinite(scale) || (clear != 0 && clear != 1))
     return VDN_ERR_INVALID_ARG;
@@ -554,7 +560,7 @@ vdn_status vdn_decay_backward(const vdn_shape* shape, const void* q, const void*
                               const float* state_in, const int* lengths, int clear, float scale, const void* dout,
                               const float* dstate_out, void* workspace, size_t workspace_bytes, void* dq, void* dk,
                               void* dv, float* dstate_in, void* stream) {
-  vdn_status st = decay_shape(shape);
+  vdn_status st = scan_shape(shape);
   if (st != VDN_OK) return st;
   if (!q || !k || !v || !decay || !dout || !workspace || !dq || !dk || !dv || !std::isfinite(scale) ||
       (clear != 0 && clear != 1))
