@@ -474,7 +474,7 @@ namespace {
 vdn_status decay_shape(const vdn_shape* sh) {
   const vdn_status s = check_shape(sh);
   if (s != VDN_OK) return s;
-  // grids of (batch, head, segment); token indices with a segment added stay in int32
+  // grids of (batch, head, segment) and of (batch, quarter of a head); token indices with a segment added stay in int32
   if ((long long)sh->B * sh->H > (1 << 24) || (long long)sh->F * sh->S > (1 << 30)) return VDN_ERR_UNSUPPORTED;
   return VDN_OK;
 }
@@ -643,7 +643,6 @@ vdn_status vdn_decay_step(const vdn_shape* shape, const void* q, const void* k, 
   if (sh.F != 1 || sh.S != 1) return VDN_ERR_INVALID_ARG;
   if (!q || !k || !v || !decay || !state || !out || n_slots < 1 || !std::isfinite(scale)) return VDN_ERR_INVALID_ARG;
   if (!slots && n_slots != sh.B) return VDN_ERR_INVALID_ARG;
-  if ((long long)sh.B * sh.H * 4 > 0x7fffffffLL) return VDN_ERR_UNSUPPORTED;
   const size_t big = token_bytes(sh);
   Buffers buf;
   buf.in(q, big);
