@@ -20,3 +20,21 @@ def test_constant_rows(dtype, d):
     y, mean, _ = api.layer_norm_forward(x, None, b, eps=1e-6)
     assert torch.equal(mean.cpu(), vals)
     assert torch.equal(y.float(), b.expand(len(vals), d))
+
+
+@pytest.mark.parametrize("d", [2, 6, 130, 514])
+def test_gradient_of_a_far_constant_row(d):
+    """fp32, x = 2^112 throughout: (x - mean) rstd is zero, and dx is rstd (g - mean g).  What lies outside the row in
+    its last vector must not enter, though 2^112 rstd there passes the fp32 range."""
+    x = torch.full((5, d), 2.0 ** 112, device="cuda")
+    g = torch.Generator("cuda").manual_seed(d)
+    dy = torch.randn(5, d, generator=g, device="cuda")
+    mean, rstd = torch.full((5,), 2.0 ** 112, device="cuda"), torch.full((5,), 2.0 ** 17, device="cuda")
+    w = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    got = api.layer_norm_backward(x, dy, mean, rstd, w, bias=True)
+    G = dy.double() * w.double()
+    ref = 2.0 ** 17 * (G - G.mean(-1, keepdim=True))
+    # the mean of g: 42 roundings of its terms' magnitudes; its product, the difference and the factor: 4
+    bound = 2.0 ** 17 * 50 * 2.0 ** -24 * (G.abs() + G.abs().mean(-1, keepdim=True))
+    assert bool(((got["dx"].double() - ref).abs() <= bound).all())
+    assert not got["dweight"].any()

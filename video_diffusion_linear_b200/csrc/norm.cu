@@ -320,29 +320,31 @@ __global__ void __launch_bounds__(block_threads<kTeam>(), kTeam > kBlock ? 1 : 2
   load(rows.first, next);
   prefetch(rows.first + rows.step);
   for (long long k = rows.first; rows.any(k, team); k += rows.step) {
-    float2 xh[kNV][kPairs], g[kNV][kPairs];
+    float2 xc[kNV][kPairs], g[kNV][kPairs];
     const float r = next.r, mu = next.mu;
     float2 s = make_float2(0.f, 0.f), s2 = s;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
       const int c = (i * kTeam + lane) * kVec - shift;
-      unpack<T>(kExact ? next.x[i] : clear_outside<T>(next.x[i], c, d), xh[i]);
+      unpack<T>(kExact ? next.x[i] : clear_outside<T>(next.x[i], c, d), xc[i]);
       unpack<T>(kExact ? next.g[i] : clear_outside<T>(next.g[i], c, d), g[i]);
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) {
-        // (x - mu) r, not x r - mu r: the difference first, where a far mean cancels.  Outside the row dy is zero.
-        xh[i][e] = __fmul2_rn(__fadd2_rn(xh[i][e], both(-mu)), both(r));
-        dw[i][e] = __ffma2_rn(g[i][e], xh[i][e], dw[i][e]);
+        // xh = (x - mu) r is not formed: r goes to dy here, to the row's sum and to dx below.  The difference comes first,
+        // where a far mean cancels.  Outside the row dy is zero, and x - mu = -mu is finite, as -mu r need not be
+        // (zero times that would be NaN).
+        xc[i][e] = __fadd2_rn(xc[i][e], both(-mu));
+        dw[i][e] = __ffma2_rn(__fmul2_rn(g[i][e], both(r)), xc[i][e], dw[i][e]);
         db[i][e] = __fadd2_rn(db[i][e], g[i][e]);
         g[i][e] = __fmul2_rn(g[i][e], w[i][e]);
         s = __fadd2_rn(s, g[i][e]);
-        s2 = __ffma2_rn(g[i][e], xh[i][e], s2);
+        s2 = __ffma2_rn(g[i][e], xc[i][e], s2);
       }
     }
     load(k + rows.step, next);
     prefetch(k + kAhead * rows.step);
     const float2 c12 = team_sum<kTeam>(make_float2(s.x + s.y, s2.x + s2.y), red, flip);
-    const float c1 = -c12.x * inv_d, c2 = -c12.y * inv_d;
+    const float c1 = -c12.x * inv_d, c2 = -(c12.y * r) * (r * inv_d);
     const long long n = rows.n(k), row = n * groups + rows.g;
     if (n >= n_rows) continue;
 #pragma unroll
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(block_threads<kTeam>(), kTeam > kBlock ? 1 : 2
       const int c = (i * kTeam + lane) * kVec - shift;
 #pragma unroll
       for (int e = 0; e < kPairs; ++e)
-        g[i][e] = __fmul2_rn(__ffma2_rn(xh[i][e], both(c2), __fadd2_rn(g[i][e], both(c1))), both(r));
+        g[i][e] = __fmul2_rn(__ffma2_rn(xc[i][e], both(c2), __fadd2_rn(g[i][e], both(c1))), both(r));
       if (kExact) *reinterpret_cast<uint4*>(dx + row * d + c) = pack<T>(g[i]);
       else if (c < d) store_cols(dx, row * d, c, d, g[i]);
     }
