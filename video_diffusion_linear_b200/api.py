@@ -603,6 +603,8 @@ def _norm_shape(x: torch.Tensor, par):
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., d]")
     dt, d = _dtype_id(x, "x"), x.shape[-1]
     pshape = (d,) if par is None or par.dim() < 2 else tuple(x.shape[-2:])
+    if max(x.shape[-2:]) > 0x7fffffff:      # the width or the groups would wrap in the library's int
+        raise _lib.VdnError(_lib.VDN_ERR_UNSUPPORTED, f"layer norm of x with shape {tuple(x.shape)}")
     return x.numel() // max(1, d), 1 if len(pshape) == 1 else pshape[0], d, pshape, dt
 
 
