@@ -1,4 +1,6 @@
 """The binding's own checks of the causal operators, beyond those of each tensor (CPU)."""
+import types
+
 import pytest
 import torch
 
@@ -20,3 +22,11 @@ def test_layer_norm_sizes_in_range_pass():
     assert api._norm_shape(x, None)[:3] == (3 * 2 ** 20, 1, 2 ** 31 - 1)
     assert api._norm_shape(x, torch.empty(3, 2 ** 31 - 1, device="meta"))[:3] == (3 * 2 ** 20, 3, 2 ** 31 - 1)
     assert api._norm_shape(torch.empty(5, 0), None)[:3] == (0, 1, 0)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The default streams of all devices have the handle 0: such a call would run on the tensors' device unordered with
+    the stream that was named."""
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
+        api._Call(torch.device("cuda", 0), stream)

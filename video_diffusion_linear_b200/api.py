@@ -456,6 +456,8 @@ class _Call:
     def __init__(self, device, stream):
         if device.type != "cuda":
             raise ValueError(f"libvdn takes CUDA tensors, got a tensor on {device}")
+        if stream is not None and stream.device != device:      # both devices' default streams have the handle 0
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         self.device, self.given = device, stream
         self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
 
