@@ -444,10 +444,10 @@ vdn_status vdn_frames_finish(const vdn_shape* shape, int F_total, int world, int
  * once: the weights lambda^{t-s} (q_t . k_s) inside a chunk of 128 tokens, and the state before the
  * chunk.  There an infinity or NaN in v inside a sequence reaches every output of its chunk (the fp32
  * path: from its token on).  Results depend neither on what ran before (no atomics) nor on whether
- * state_out is taken.  Calls that may run at the same time, captured graphs among them, need workspaces of
- * their own.  Errors as
- * vdn_branch_forward; vdn_shape's conv_width is not used (1 or 3).  VDN_ERR_UNSUPPORTED: other d and
- * dtype, B*H above 2^24, more than 2^30 tokens.
+ * state_out is taken.  Calls that may run at the same time, captured graphs among them, need
+ * workspaces of their own.  Errors as vdn_branch_forward; vdn_shape's conv_width is not used (1 or 3).
+ * VDN_ERR_UNSUPPORTED: other d and dtype, bf16 in a build without the tensor-core path, B*H above 2^24,
+ * more than 2^30 tokens.
  */
 size_t vdn_decay_workspace_size(const vdn_shape* shape);
 vdn_status vdn_decay_forward(const vdn_shape* shape, const void* q, const void* k, const void* v,
@@ -462,6 +462,7 @@ vdn_status vdn_decay_forward(const vdn_shape* shape, const void* q, const void* 
  * The forward's states are recomputed from k and v; nothing is saved between the calls.  In a call
  * with a state_in no result depends on which optional outputs are taken.  bf16 without one: asking for
  * dstate_in keeps the state's gradient more exactly, which can change the last bits of dk and dv.
+ * What the forward says of v in a chunk holds here for k in dq, for q in dk and for dout in dv.
  * workspace: vdn_decay_backward_workspace_size() bytes.  No output may overlap another
  * buffer. */
 size_t vdn_decay_backward_workspace_size(const vdn_shape* shape);

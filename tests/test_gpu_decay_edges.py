@@ -86,3 +86,46 @@ def test_sequences_that_end_at_every_place_of_a_chunk(first):
             have = grads[what].double().cpu().numpy()[b]
             assert bool((have[n:] == -77.0).all())
             within(have[:n], rg[what][0], bd[0], (what, b))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,d,T", [("bf16", 128, 300), ("bf16", 128, 1700), ("f32", 128, 300), ("f32", 16, 300)])
+def test_what_an_infinite_token_reaches(dtype, d, T, value):
+    """The results that an infinity or NaN in one token of an operand leaves alone keep their bits.  fp32: all before it
+    (from the end: behind it).  bf16: the same, but for the operand whose terms the output sums (v; in the gradients k,
+    q and dout): there the whole chunk of 128 tokens is reached."""
+    t, chunk = 200, (128, 256)
+    x = cuda(inputs(33, dtype, 2, T, 2, d))
+    x["decay"] = torch.tensor([0.97, 0.9], device="cuda")
+
+    def call(y):
+        args = (y["q"], y["k"], y["v"], y["decay"], y["state"])
+        out, last = api.decay_forward(*args)
+        g = api.decay_backward(*args, dout=y["dout"], dfinal=y["dfinal"])
+        return {"out": out, "state": last, **g}
+
+    clean = call(x)
+    # result: the operand read at the output's token, the two that are summed, the second of them into the output
+    roles = {"out": ("q", "k", "v", False), "dq": ("dout", "v", "k", False), "dk": ("v", "dout", "q", True),
+             "dv": ("k", "q", "dout", True)}
+    for name in ("q", "k", "v", "dout"):
+        y = {**x, name: x[name].clone()}
+        y[name][0, t, 0, 3] = value
+        got = call(y)
+        for result, (own, key, term, reverse) in roles.items():
+            reached = torch.zeros(T, dtype=torch.bool)
+            if name == own:
+                reached[t] = True
+            if name in (key, term):
+                reached[:t + 1] |= reverse
+                reached[t:] |= not reverse
+                if name == term and dtype == "bf16":
+                    reached[chunk[0]:chunk[1]] = True
+            reached = reached.cuda()
+            assert torch.equal(got[result][0, ~reached, 0], clean[result][0, ~reached, 0]), (name, result)
+            assert not bool(torch.isfinite(got[result][0, t, 0]).all()) or not bool(reached[t]), (name, result)
+            assert torch.equal(got[result][1], clean[result][1]) and torch.equal(got[result][0, :, 1], clean[result][0, :, 1])
+        for result, operands in (("state", "k v"), ("dstate", "q dout")):
+            assert torch.equal(got[result][1], clean[result][1]) and torch.equal(got[result][0, 1], clean[result][0, 1])
+            if name not in operands.split():
+                assert torch.equal(got[result], clean[result]), (name, result)
