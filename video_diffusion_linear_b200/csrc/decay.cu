@@ -17,9 +17,9 @@ namespace vdn {
 // 8 x 16 spends 160 cycles on loads and 384 on arithmetic per token, 2 x 64 512 on loads).  The chunked form has no
 // fewer operations here: its products with the state cost the same 4 d^2 per token, and without tensor cores the near
 // terms come on top.  Few rows leave an SM one unit of four warps, so a token's chain of loads, multiply-adds and
-// shuffles bounds it: 0.28 us per token with its output, 0.18 without (d = 128).  Forward and backward of 2 x
-// 777 tokens x 4 heads: 113 us, 14 us of them arithmetic at the fp32 rate (119 with tiles of 4 tokens, a barrier each;
-// 129 with one token at a time).
+// shuffles bounds it: 0.28 us per token with its output, 0.18 without (d = 128).  The gradients of 2 x 777 tokens x 4
+// heads (five launches of up to 128 blocks and two prefixes): 114 us, 14 us of them arithmetic at the fp32 rate (5 %
+// more with tiles of 4 tokens, a barrier each; 14 % with one token at a time).
 namespace {
 
 template <int D> struct ScanShape;
@@ -317,11 +317,12 @@ cudaError_t launch_decay_prefix(const DecayScan& s, const DecayPlan& p, float* s
 // One pass over the state: S <- lambda S + v k^T, o = scale S q.  Bound by the state's bytes (2 x 64 KB
 // per row and head at d = 128).  A warp takes eight rows, a row per load instruction (512 bytes), all
 // eight loads in flight before the first use; a (row of the batch, head) is split over four CTAs so that
-// a single sequence still reaches most SMs.  256 rows x 24 heads: 131 us, 6.2 TB/s; one row x 24 heads: 6 us
-// with a cold L2, below the 10 us that the binding takes to issue it.
+// a single sequence still reaches most SMs.  256 rows x 24 heads: 132 us, 6.1 TB/s, bf16 and fp32 alike; one row x 24
+// heads: 6 us with a cold L2, below the 10 us that the binding takes to issue it.
 //
 // With slots, the state of row b lies in slot slots[b].  The CTA of the first row that names a slot
-// takes every later row of that slot too, in row order: they are steps of one sequence.
+// takes every later row of that slot too, in row order: they are steps of one sequence.  Every CTA looks through all
+// slots for that (B / 128 loads a thread: nothing against its 8 KB of state, but for thousands of rows with small states).
 namespace {
 
 constexpr int kStepThreads = 128;
@@ -418,8 +419,12 @@ cudaError_t launch_decay_step(const vdn_shape& sh, const void* q, const void* k,
 // v; more fill the SMs when there are few rows.  The choice is the smallest estimate of
 //   waves(rows) (start + units scan)                                    (one segment)
 //   waves(rows nseg) (2 start + units / nseg (scan + own)) + rest       (split: own states, prefix, scan)
-// with measured times per unit (a chunk of 128 tokens, or a token) and per block: a split pays from 1024 tokens
-// on the tensor-core path with two heads (20 us against 36 us) and never with 148 rows or more.
+// with measured times per unit (a chunk of 128 tokens, or a token) and per block, for the forward; the gradients take
+// the same segments.  A split pays from 1024 tokens on the tensor-core path with two heads (20 us against 36 us), and
+// above 148 rows too where the last wave of one pass would be poorly filled.  There, split against one pass, forward
+// and gradients in us: fp32 160 rows of 2048 tokens 1120 against 1324 and 2890 against 3945; bf16 150 rows of 20000
+// 1030 against 1070 and 2610 against 2880, but 150 rows of 8192 459 against 435 and 1169 against 1154.  It goes by the
+// padded length: the lengths are on the device.  fp32, d = 128: two blocks fit an SM, the estimate counts one.
 struct DecayCost {
   int unit, least, slots;          // tokens per unit, units per segment at least, segments that run at once
   double start, scan, own, rest;   // microseconds

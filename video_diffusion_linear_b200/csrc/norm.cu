@@ -4,13 +4,13 @@
 //   mu = mean x, rstd = (mean (x - mu)^2 + eps)^-1/2, xh = (x - mu) rstd, y = xh w + b
 //   g = dy w:  dx = rstd (g - mean g - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy
 //
-// Bound by the bytes of x, y (dy, dx): each is read or written once.  A team of threads keeps a whole row
-// in registers, so the variance is taken about the mean in a second sweep of registers (no
+// Bound by the bytes of x, y (dy, dx): each is read or written once.  A team of threads holds a whole row
+// (in registers, but for the spills named below), so the variance is taken about the mean in a second sweep (no
 // sum-of-squares cancellation).  A block walks rows of one group, so that a thread meets the same columns in
 // all of them: weight and bias stay in registers, and in the backward its part of dw and db too; blocks leave
 // partial sums that a second kernel adds in a fixed order.  A row's vectors are requested while the row before is
-// worked on, and lines of the rows after that are brought into L2 (48360 x 24 rows of 128: 111 -> 97 us forward,
-// 209 -> 181 us backward).  Small teams with two (fp32: four) vectors per thread beat a team twice as large with one:
+// worked on, and lines of the rows after that are brought into L2 (48360 x 24 rows of 128, bf16: 13 % off the forward
+// and the backward).  Small teams with two (fp32: four) vectors per thread beat a team twice as large with one:
 // fewer shuffles, and fewer addresses per element, which is what the kernels issue besides the arithmetic.
 //
 // All accesses are 16-byte vectors, whatever the width: where a row does not start on 16 bytes, the
@@ -18,7 +18,13 @@
 // -- so that its columns stay in place.  Vectors that reach outside a row are stored by elements, and one
 // that would reach past the tensor's end is loaded by elements.
 //
-// Measured with a cold L2, 48360 x 24 rows of 128, bf16: forward 102 us, 5.9 TB/s; backward 166 us, 5.4 TB/s.
+// Measured with a cold L2 and buffers given, 48360 x 24 rows of 128: bf16 forward 102 us, 5.8 TB/s, backward 169 us,
+// 5.3 TB/s; fp32 190 us, 6.2 TB/s, and 310 us, 5.7 TB/s.
+//
+// Spilled bytes a thread (stores): forward none up to 8192 wide, beyond (teams of 1024, 64 registers) 84 - 516; backward
+// bf16 none at the widths of whole teams and 8 - 80 at others, fp32 12 - 124 and 68 - 276, beyond 8192 up to 1128.  They
+// cost the long rows most: 3000 rows of 16384, fp32, take 162 us and 366 us (2.4 and 1.6 TB/s); 3000 of 8192, bf16,
+// 33 us and 52 us (3.0 and 2.8 TB/s).
 #include <cmath>
 
 #include "check.h"
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(block_threads<kTeam>())
         s2 = __fadd2_rn(s2, v[i][e]);
     // Divided, not times 1 / d: where the sum is exact (a constant row of few digits) so is the mean, at any width, and
     // the centred row is zero instead of the mean's rounding times a large rstd.  kExact has a power of two for d,
-    // where the product is the quotient (the division there: 110.0 -> 111.7 us for 48360 x 24 rows of 128).
+    // where the product is the quotient (the division costs 1.5 % there: 48360 x 24 rows of 128).
     const float sum = team_sum<kTeam>(s2.x + s2.y, red, flip), mu = kExact ? sum * inv_d : sum / (float)d;
     s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -454,11 +460,11 @@ template <template <typename, int, int, bool> class Op, typename T, typename A> 
 
 // Blocks per group: `threads` per SM over all groups, and no more than have a row; a multiple of the classes of rows
 // (at least one block each).  Every block reads its parameters first, and in the backward leaves a partial sum.
-// Long rows (teams of a warp or more): two blocks, which run at once; with four, 4032 rows of 1999 take 29 us
-// instead of 25 in the backward, 3000 of 8192 75 instead of 64.  Short rows, whose parameters are short: several
-// times that, so that the last blocks end together (48360 x 24 rows of 128, backward: 158 us with 12 blocks, 180 with
-// four; forward 97 with 24, 103 with eight; inputs in turn), but a third of it where rows start at odd places and
-// parameters are read one by one (100000 rows of 77: 23 us against 32).
+// Long rows (teams of a warp or more): two blocks, which run at once; with four, the backward takes 16 % longer for
+// 4032 rows of 1999 and 17 % for 3000 of 8192.  Short rows, whose parameters are short: several times that, so that
+// the last blocks end together (48360 x 24 rows of 128: backward 12 % less with 12 blocks than with four, forward 6 % less
+// with 24 than with eight; inputs in turn), but a third of it where rows start at odd places and parameters are read
+// one by one (100000 rows of 77: 28 % less).
 struct NormThreads {
   int long_rows, short_rows, short_odd;
 };

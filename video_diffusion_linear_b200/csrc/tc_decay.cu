@@ -21,9 +21,9 @@
 // with A in either place, 90 - 100 while the other units work too.
 //
 // Bound by the chain of dependent steps within a chunk, not by one unit: X Y^T -> weights -> P Z -> output on one
-// side, keys -> their product -> state -> X S^T on the other, about 6000 cycles per chunk, products 38 - 46 % of
-// them and DRAM at 57 - 62 % of its rate: 60 us for 12288 tokens x 24 heads; all of a call, 48360 tokens: forward
-// 418 us, gradients (five passes) 996.  What counts besides is the code of a chunk, which the warps' roles fetch from
+// side, keys -> their product -> state -> X S^T on the other, about 6000 cycles per chunk, products 39 - 47 % of
+// them and DRAM at 52 - 57 % of its rate: 59 - 61 us for 12288 tokens x 24 heads; all of a call, 48360 tokens: forward
+// 400 - 430 us, gradients (five passes) 940 - 1020, by the clock that the power cap leaves.  What counts besides is the code of a chunk, which the warps' roles fetch from
 // different places: loops that are not unrolled and one instance of each step brought 72 us (three terms) and 67
 // (reverse) to 60 and 59.  What was tried and is slower: fewer, fuller warps (4 + 8), waits that suspend the thread
 // (+ 2.5 %) or are called, the state's part decayed by the state's warps, both halves of a row loaded at once (spills).
@@ -628,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- states of the segments
 // The state that a segment's own tokens leave at its end: the scan's state part alone.  Bound by the warps' work on the
-// keys with three terms (2950 cycles per chunk, products 50 % of them), by them and DRAM (60 % of its rate) with two:
-// 30 us and 26 us for 12288 tokens x 24 heads.  Bringing later chunks into L2 ahead of their loads is slower, here and
+// keys with three terms (2950 cycles per chunk, products 51 % of them), by them and DRAM (58 % of its rate) with two:
+// 30 us and 26 - 29 us for 12288 tokens x 24 heads.  Bringing later chunks into L2 ahead of their loads is slower, here and
 // in the scan (two chunks ahead: 32 and 60 us; four: 35 and 77), and so is one instance of `keys` for both halves (33).
 namespace {
 
